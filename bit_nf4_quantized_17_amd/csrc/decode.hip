@@ -56,7 +56,7 @@
 // 64 tokens; rows of other adapters are not loaded).  In the stream kernel
 // wave w takes every eighth of the adapters from the w-th on: its factor's
 // rows come straight from HBM into MFMA operands, the product with all
-// tokens' bf16(scale T) is summed apart and added to the adapter's own rows,
+// tokens' scale T (two bf16 terms, 2^-16 left out) is summed apart and added to the adapter's own rows,
 // so no factor reaches another's tokens; the waves' sums then add up as
 // before.  K is any multiple of 64 here: a row may end in half a chunk, whose
 // second block meets zero activations and zero scales (4 tokens, 5019x2688:
@@ -678,12 +678,18 @@ __global__ __launch_bounds__(NTHREADS) void k_decode(DecArgs p) {
       if (f_any) load_factor(fb, f_id, c);
       const f32x4_t* tr = reinterpret_cast<const f32x4_t*>(ttab + i16 * MAX_R + 32u * c0 + 8u * (uint32_t)g);
       const f32x4_t ta = tr[0], tb = tr[1];
-      const u32x4v tv = {pack_bf16x2(ta[0], ta[1]), pack_bf16x2(ta[2], ta[3]), pack_bf16x2(tb[0], tb[1]),
-                         pack_bf16x2(tb[2], tb[3])};
+      uint32_t hi[4], lo[4];
+      split_bf16x2(ta[0], ta[1], hi[0], lo[0]);
+      split_bf16x2(ta[2], ta[3], hi[1], lo[1]);
+      split_bf16x2(tb[0], tb[1], hi[2], lo[2]);
+      split_bf16x2(tb[2], tb[3], hi[3], lo[3]);
+      const u32x4v th = {hi[0], hi[1], hi[2], hi[3]}, tl = {lo[0], lo[1], lo[2], lo[3]};
 #pragma unroll
       for (int t = 0; t < TR; ++t) {
         f32x4_t y = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tv), __builtin_bit_cast(bf16x8_t, cur[t]), y, 0, 0, 0);
+        const bf16x8_t f = __builtin_bit_cast(bf16x8_t, cur[t]);
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, th), f, y, 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tl), f, y, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] += (own >> e) & 1u ? y[e] : 0.0f;
       }

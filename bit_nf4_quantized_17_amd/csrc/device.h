@@ -26,6 +26,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float x) {
   return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
+// Two fp32 as packed bf16 pairs of their nearest and of what it leaves over: 2^-16
+// of a value is left out.  Behind an infinity the rest is zero, not NaN.
+__device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x0, x1);
+  const float r0 = x0 - __uint_as_float(hi << 16), r1 = x1 - __uint_as_float(hi & 0xFFFF0000u);
+  lo = pack_bf16x2(fabsf(r0) < __builtin_inff() ? r0 : 0.0f, fabsf(r1) < __builtin_inff() ? r1 : 0.0f);
+}
+
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) {
   return __uint_as_float((uint32_t)h << 16);
 }

@@ -638,43 +638,51 @@ __global__ __launch_bounds__(NTHREADS) void k_gemm(GemmArgs p) {
         ProdT<BN> lbt;
         if constexpr (LORA == LORA_FWD) lbc.load(fac, p.r, p.J, p.r, j0, c0, p.lb_vec, tid);
         else lbt.load(fac, p.J, p.r, p.J, j0, c0, p.lb_vec, tid);
-        __syncthreads();
+        // the rows' operand as two bf16 terms, one after the other through sA
+#pragma unroll 1
+        for (int term = 0; term < 2; ++term) {
+          __syncthreads();
 #pragma unroll
-        for (int q = 0; q < BM / 32; ++q) {
-          const int64_t pos = i0 + tid / 8 + 32 * q, c = c0 + (tid % 8) * 8;
-          float x[8];
-          const bool in = pos >= q0 && pos < q1;
-          const float* src = p.la + (in ? (int64_t)p.mo.perm[pos] : 0) * p.r;
+          for (int q = 0; q < BM / 32; ++q) {
+            const int64_t pos = i0 + tid / 8 + 32 * q, c = c0 + (tid % 8) * 8;
+            float x[8];
+            uint32_t hi[4], lo[4];
+            const bool in = pos >= q0 && pos < q1;
+            const float* src = p.la + (in ? (int64_t)p.mo.perm[pos] : 0) * p.r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = in && c + e < p.r ? sc * src[c + e] : 0.0f;
-          *reinterpret_cast<uint4*>(sA + (tid / 8 + 32 * q) * PITCH + (tid % 8) * 8) =
-              make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                         pack_bf16x2(x[6], x[7]));
-        }
-        if constexpr (LORA == LORA_FWD) lbc.store(sB, tid);
-        else lbt.store(sB, tid);
-        __syncthreads();
+            for (int e = 0; e < 8; ++e) x[e] = in && c + e < p.r ? sc * src[c + e] : 0.0f;
 #pragma unroll
-        for (int a = 0; a < TM; ++a)
-#pragma unroll
-          for (int b = 0; b < TN; ++b) {
-            f32x16_t t;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) t[v] = 0.0f;
-#pragma unroll
-            for (int ks = 0; ks < BK / 16; ++ks) {
-              const bf16x8_t fa = *reinterpret_cast<const bf16x8_t*>(
-                  sA + (wm * (BM / WM) + a * 32 + (lane & 31)) * PITCH + ks * 16 + (lane >> 5) * 8);
-              const bf16x8_t fb = *reinterpret_cast<const bf16x8_t*>(
-                  sB + (wn * (BN / WN) + b * 32 + (lane & 31)) * PITCH + ks * 16 + (lane >> 5) * 8);
-              t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, t, 0, 0, 0);
-            }
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const int64_t pos = i0 + wm * (BM / WM) + a * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-              acc[a][b][v] += pos >= q0 && pos < q1 ? t[v] : 0.0f;
-            }
+            for (int e = 0; e < 4; ++e) split_bf16x2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+            *reinterpret_cast<uint4*>(sA + (tid / 8 + 32 * q) * PITCH + (tid % 8) * 8) =
+                make_uint4(term ? lo[0] : hi[0], term ? lo[1] : hi[1], term ? lo[2] : hi[2], term ? lo[3] : hi[3]);
           }
+          if (term == 0) {
+            if constexpr (LORA == LORA_FWD) lbc.store(sB, tid);
+            else lbt.store(sB, tid);
+          }
+          __syncthreads();
+#pragma unroll
+          for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int b = 0; b < TN; ++b) {
+              f32x16_t t;
+#pragma unroll
+              for (int v = 0; v < 16; ++v) t[v] = 0.0f;
+#pragma unroll
+              for (int ks = 0; ks < BK / 16; ++ks) {
+                const bf16x8_t fa = *reinterpret_cast<const bf16x8_t*>(
+                    sA + (wm * (BM / WM) + a * 32 + (lane & 31)) * PITCH + ks * 16 + (lane >> 5) * 8);
+                const bf16x8_t fb = *reinterpret_cast<const bf16x8_t*>(
+                    sB + (wn * (BN / WN) + b * 32 + (lane & 31)) * PITCH + ks * 16 + (lane >> 5) * 8);
+                t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, t, 0, 0, 0);
+              }
+#pragma unroll
+              for (int v = 0; v < 16; ++v) {
+                const int64_t pos = i0 + wm * (BM / WM) + a * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+                acc[a][b][v] += pos >= q0 && pos < q1 ? t[v] : 0.0f;
+              }
+            }
+        }
       }
       q0 = q1;
     }

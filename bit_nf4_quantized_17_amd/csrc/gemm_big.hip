@@ -41,8 +41,11 @@
 //
 // Many adapters (MULTI): a tile's 256 rows are 256 positions of the order
 // sorted by adapter (multi.hip), read and written through it.  The A side of
-// the prologue, bf16(scale T) of each row, does not depend on the adapter
-// whose factor it meets, so it is staged once per 64 ranks; the factors of
+// the prologue, scale T of each row, does not depend on the adapter
+// whose factor it meets, so it is staged once per 64 ranks, as two bf16
+// terms (the rest of the first in the second: 2^-16 left out, as dA and dB
+// leave out of T and U; with the first term alone the rounding of scale T was
+// as large an error as that of the output); the factors of
 // the tile's runs are staged after it, as many as fit the 64-deep stage
 // (four of rank <= 16, two of rank <= 32), the next ones loaded while these
 // multiply.  A run's product of a 32 x 32 block is summed apart and added to
@@ -315,11 +318,11 @@ struct RunTable {
 };
 
 // Many adapters, A side of the prologue: row t is position m0 + t, its own T
-// or U times its own adapter's scale, rounded to bf16 (zeros for a row without
+// or U times its own adapter's scale, as two bf16 terms (zeros for a row without
 // an adapter or past M).
 template <int TMB>
-__device__ __forceinline__ void lora_a_tile_multi(const BigArgs& p, const RunTable* rt, int c0, bool save, u16* sA,
-                                                  int tid) {
+__device__ __forceinline__ void lora_a_tile_multi(const BigArgs& p, const RunTable* rt, int c0, bool save, u16* sHi,
+                                                  u16* sLo, int tid) {
 #pragma unroll 2
   for (int q = 0; q < TMB; ++q) {
     const int t = tid / 8 + 64 * q, c = c0 + (tid % 8) * 8;
@@ -364,9 +367,12 @@ __device__ __forceinline__ void lora_a_tile_multi(const BigArgs& p, const RunTab
       if (save && row >= 0 && c + e < p.r) p.t_save[row * p.r + c + e] = x[e];
       x[e] *= sc;
     }
-    *reinterpret_cast<uint4*>(sA + (tid / 8 + 64 * q) * APITCH + (tid % 8) * 8) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                   pack_bf16x2(x[6], x[7]));
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_bf16x2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+    const int at = (tid / 8 + 64 * q) * APITCH + (tid % 8) * 8;
+    *reinterpret_cast<uint4*>(sHi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(sLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -673,8 +679,9 @@ __global__ __launch_bounds__(NTHREADS, 1) void k_gemm_big(BigArgs p) {
 
   // ---- LoRA prologue, many adapters ----
   if constexpr (MULTI) {
-    RunTable* rt = reinterpret_cast<RunTable*>(sA[1]);   // free until the main loop's first store
+    __shared__ RunTable s_runs;
     __shared__ int s_wave[TMB];
+    RunTable* rt = &s_runs;
     const int mine = tid < ROWS ? (m0 + tid < p.M ? p.mo.sid[m0 + tid] : p.mo.count) : p.mo.count;
     const int before = tid > 0 && tid < ROWS ? (m0 + tid - 1 < p.M ? p.mo.sid[m0 + tid - 1] : p.mo.count) : -1;
     const bool first = tid < ROWS && mine != before;   // the rows without an adapter are the last run
@@ -720,7 +727,7 @@ __global__ __launch_bounds__(NTHREADS, 1) void k_gemm_big(BigArgs p) {
         for (int q = 0; q < 4; ++q) v[q] = load_lora_b_multi<MODE, VEC>(p, rt, uhi, u, rp, j0, c0, tid, q);
       };
       if (c0 > 0) __syncthreads();   // the last chunk's fragments are read
-      lora_a_tile_multi<TMB>(p, rt, c0, save, sA[0], tid);
+      lora_a_tile_multi<TMB>(p, rt, c0, save, sA[0], sA[1], tid);
       ahead(ulo);
       int buf = 0;
       for (int u0 = ulo; u0 < uhi; u0 += slots, buf ^= 1) {
@@ -754,9 +761,10 @@ __global__ __launch_bounds__(NTHREADS, 1) void k_gemm_big(BigArgs p) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) tmp[i] = 0.0f;
               for (int ks = k0; ks < k1; ++ks) {
-                const bf16x8_t fa = *reinterpret_cast<const bf16x8_t*>(
-                    sA[0] + (wm * WROWS + a * 32 + (lane & 31)) * APITCH + (ks - k0) * 16 + (lane >> 5) * 8);
-                tmp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, read_b<MODE>(sBc, wn, b, ks, lane), tmp, 0, 0, 0);
+                const int at = (wm * WROWS + a * 32 + (lane & 31)) * APITCH + (ks - k0) * 16 + (lane >> 5) * 8;
+                const bf16x8_t fb = read_b<MODE>(sBc, wn, b, ks, lane);
+                tmp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8_t*>(sA[0] + at), fb, tmp, 0, 0, 0);
+                tmp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8_t*>(sA[1] + at), fb, tmp, 0, 0, 0);
               }
 #pragma unroll
               for (int i = 0; i < 16; ++i) {

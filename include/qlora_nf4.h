@@ -330,11 +330,13 @@ typedef struct {
  * task; Ultralytics "QLoRA": the base stays frozen in 4 bits).  With a =
  * ids[m], in any order, tokens of one adapter together or not:
  *   T_save[m] = X[m] A[a]^T                                      fp32 [M][r]
- *   Y[m]      = bf16(X[m] W'^T + bf16(scale[a] T[m]) B[a]^T)          [M][N]
- * A value of ids [M] (device) outside 0 .. count - 1, such as -1, means no
- * adapter: T is zero and Y the base product.  A row depends on its own input
- * and adapter only: a NaN or infinity in another token's row or adapter does
- * not reach it.  Other arguments as in qlora_linear_fwd.
+ *   Y[m]      = bf16(X[m] W'^T + (scale[a] T[m]) B[a]^T)              [M][N]
+ * scale[a] T[m] meets B as two bf16 terms, all but 2^-16 of it
+ * (qlora_linear_fwd rounds its own to one).  A value of ids [M] (device)
+ * outside 0 .. count - 1, such as -1, means no adapter: T is zero and Y the
+ * base product.  A row depends on its own input and adapter only: a NaN or
+ * infinity in another token's row or adapter does not reach it.  Other
+ * arguments as in qlora_linear_fwd.
  * workspace: device, at least qlora_multi_fwd_workspace_bytes(...) bytes. */
 size_t qlora_multi_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int count);
 int qlora_multi_fwd(const qlora_nf4_weight* w, const uint16_t* X, int64_t M,
@@ -344,9 +346,10 @@ int qlora_multi_fwd(const qlora_nf4_weight* w, const uint16_t* X, int64_t M,
 
 /* Backward of qlora_multi_fwd, for training several adapters of one weight
  * in one batch.  With U[m] = dY[m] B[a] (fp32):
- *   dX[m] = bf16(dY[m] W' + bf16(scale[a] U[m]) A[a])                [M][K]
+ *   dX[m] = bf16(dY[m] W' + (scale[a] U[m]) A[a])                    [M][K]
  *   dA[a] = bf16(scale[a] sum_{m: ids[m] = a} U[m]^T X[m])     [count][r][K]
  *   dB[a] = bf16(scale[a] sum_{m: ids[m] = a} dY[m]^T T[m])    [count][N][r]
+ * scale[a] U[m], U[m] and T[m] enter these products as two bf16 terms.
  * Sums run over an adapter's tokens in a fixed order.  An adapter that no
  * token names gets zero gradients; tokens without an adapter add to none.
  * T_saved: the forward's T_save, or NULL to recompute it.  dX may be NULL
