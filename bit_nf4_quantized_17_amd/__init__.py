@@ -658,12 +658,16 @@ def _explain_adamw8(params, grads, states, masters, dev):
 
 
 def qlora_adamw8_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
-                      weight_decay: float = 0.0, step: int = 1, seed: int = 0, masters=None,
+                      weight_decay: float = 0.0, step: int = 1, seed: Optional[int] = None, masters=None,
                       stream=None) -> None:
     """One AdamW step over lists of tensors, in place, with 8-bit moments: bf16
     params and grads, AdamW8State per tensor, optional fp32 masters (None
-    entries allowed).  seed (32 bits) drives the stochastic rounding of the
-    second moment; pass another one every step."""
+    entries allowed).  seed (32 bits; the step number if None) drives the
+    stochastic rounding of the second moment.  It has to differ from step to
+    step: under one seed an element meets the same threshold every time, and a
+    second moment that shrinks by less than a code a step stays where it is.
+    A captured call replays its seed and its step's bias correction, so a graph
+    is one step, not a loop's."""
     import torch
     n = len(params)
     masters = masters if masters is not None else [None] * n
@@ -671,6 +675,7 @@ def qlora_adamw8_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps:
         raise ValueError("tensor lists differ in length")
     if n == 0:
         return
+    seed = step if seed is None else seed
     dev = params[0].device
     table = _native().adamw8(list(params), list(grads), list(states), list(masters),
                              dev.index if dev.type == "cuda" else -1)

@@ -300,7 +300,10 @@ typedef struct {
  * up with the probability of its distance, by 16 bits of
  * a hash of `seed` and of the element's place in the whole list (each tensor
  * counted in whole blocks).  The same seed gives the same bits again; a
- * training loop passes another seed every step (its step number will do).
+ * training loop has to pass another seed every step (its step number will do):
+ * under one seed an element meets the same threshold every time, and u stays
+ * up after gradients that shrink (several times too large).  A captured call
+ * replays its seed and its step's bias correction: the graph is that one step.
  * Hyperparameters are doubles, each coefficient rounded to fp32 once.
  * A tensor stands in the list once, and no two share codes or scales; scales
  * need 4-byte alignment, all else 16.  step >= 1; 0 <= beta < 1; eps > 0 (a
