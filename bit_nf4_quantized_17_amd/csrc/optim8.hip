@@ -10,7 +10,9 @@
 //   theta' = theta (1 - lr wd) - (lr / (1 - b1^t)) m' / (u' / sqrt(1 - b2^t) + eps)
 //   dm' = max|m'| / 448,   cm' = E4M3 nearest(m' 448 / max|m'|)
 //   du' = max u' / 448,    cu' = E4M3 stochastic(u' 448 / max u'), at least 1 if u' > 0
-// (a block with max|m'| < 2^-117 has dm' = cm' = 0),
+// (a block with max|m'| < 2^-117 has dm' = cm' = 0; an element whose m' or u'
+// is not finite has the NaN code there and counts in no maximum, so a gradient
+// of NaN or infinity stays its own element's: blocks cross rows, and adapters),
 //
 // in fp32, every operation rounded on its own (this file is compiled without
 // contraction, so the stored bits are defined by these lines).  The update
@@ -146,18 +148,41 @@ __global__ __launch_bounds__(NTHREADS) void k_adamw8(Args a) {
     }
   }
 
+  constexpr float INF = __builtin_inff();
   float m[EPT], u[EPT], am = 0.0f, au = 0.0f;
+  auto grad = [&](int e) { return __uint_as_float(e & 1 ? gw[e >> 1] & 0xFFFF0000u : gw[e >> 1] << 16); };
+  auto root = [&](int e) { return __builtin_amdgcn_cvt_f32_fp8((int)(uw[e >> 2] >> (8 * (e & 3))), 0) * du; };
+  uint32_t top = 0;   // of the variances' bits (not negative): infinity and NaN are the largest
 #pragma unroll
   for (int e = 0; e < EPT; ++e) {
-    const float g = __uint_as_float(e & 1 ? gw[e >> 1] & 0xFFFF0000u : gw[e >> 1] << 16);
+    const float g = grad(e), uo = root(e);
     if constexpr (!MASTER) th[e] = __uint_as_float(e & 1 ? pw[e >> 1] & 0xFFFF0000u : pw[e >> 1] << 16);
     m[e] = a.b1 * (__builtin_amdgcn_cvt_f32_fp8((int)(mw[e >> 2] >> (8 * (e & 3))), 0) * dm) + a.c1 * g;
-    const float uo = __builtin_amdgcn_cvt_f32_fp8((int)(uw[e >> 2] >> (8 * (e & 3))), 0) * du;
-    u[e] = __builtin_sqrtf(a.b2 * (uo * uo) + a.c2 * (g * g));
-    th[e] = th[e] * a.decay - a.step_size * (m[e] / (u[e] * a.inv_sqrt_bc2 + a.eps));
+    const float v = a.b2 * (uo * uo) + a.c2 * (g * g);
+    top = max(top, __float_as_uint(v));
+    u[e] = __builtin_sqrtf(v);
     am = fmaxf(am, fabsf(m[e]));
-    au = fmaxf(au, u[e]);
   }
+  au = __builtin_sqrtf(__uint_as_float(top));
+  // whether an m or v of this lane is not finite (fmaxf drops a NaN; m's come from a
+  // gradient's, which v has too, or from a code): found by the lane (by the element 70.8M
+  // parameters took 178 us for 166)
+  auto nan_code = [](uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
+  const bool odd = !(au < INF) || !(am < INF) || !(dm < INF) || (nan_code(mw[0]) | nan_code(mw[1])) != 0;
+  if (odd) {
+    am = au = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      if (!(u[e] < INF)) {   // g over 2^64: the same root of numbers 2^64 times smaller
+        const float g = grad(e) * 0x1p-64f, uo = root(e) * 0x1p-64f;
+        u[e] = __builtin_sqrtf(a.b2 * (uo * uo) + a.c2 * (g * g)) * 0x1p64f;
+      }
+      if (fabsf(m[e]) < INF) am = fmaxf(am, fabsf(m[e]));
+      if (u[e] < INF) au = fmaxf(au, u[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) th[e] = th[e] * a.decay - a.step_size * (m[e] / (u[e] * a.inv_sqrt_bc2 + a.eps));
   am = max32(am);
   au = max32(au);
   am = am >= LEAST ? am : 0.0f;
@@ -175,6 +200,14 @@ __global__ __launch_bounds__(NTHREADS) void k_adamw8(Args a) {
     op[e >> 1] = pack_bf16x2(th[e], th[e + 1]);
   }
 
+  if (odd) {   // 0x7F, the NaN code, over what is not finite
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const int at = 8 * (e & 3);
+      if (!(fabsf(m[e]) < INF)) om[e >> 2] = (om[e >> 2] & ~(0x80u << at)) | 0x7Fu << at;
+      if (!(u[e] < INF)) ou[e >> 2] |= 0x7Fu << at;
+    }
+  }
   if (left > 0 && e0 % BLK == 0) {
     T.sm[blk] = am * (1.0f / 448.0f);
     T.su[blk] = au * (1.0f / 448.0f);

@@ -308,8 +308,9 @@ typedef struct {
  * A tensor stands in the list once, and no two share codes or scales; scales
  * need 4-byte alignment, all else 16.  step >= 1; 0 <= beta < 1; eps > 0 (a
  * variance below fp32's range is kept as zero).  count and numel may be 0
- * (numel at most 2^34).  Gradients are finite, with squares inside fp32's range: what is not turns
- * its block's scale infinite, and the block NaN. */
+ * (numel at most 2^34).  A gradient of NaN or infinity makes its own element NaN:
+ * the parameter, the master and, for good, both codes (0x7F).  Scales are those
+ * of the finite elements, so no other element of the block changes. */
 int qlora_adamw8_step(const qlora_adamw8_tensor* tensors, int count, double lr, double beta1,
                       double beta2, double eps, double weight_decay, int64_t step, uint32_t seed,
                       void* stream);
