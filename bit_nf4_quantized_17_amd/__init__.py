@@ -649,7 +649,7 @@ def _explain_adamw8(params, grads, states, masters, dev):
         if w is not None:
             _need_on(w, torch.float32, p.shape, f"masters[{i}]", dev)
         for t, name in ((p, "params"), (s.exp_avg, "states"), (s.exp_root, "states"), (w, "masters")):
-            if t is None or not t.numel() or not t.data_ptr():   # (a tracer's have no address)
+            if t is None or not t.numel() or not _native().has_memory(t):   # (a tracer's have no address to ask for)
                 continue
             if t.data_ptr() in seen:
                 raise ValueError(f"{name}[{i}]: the same tensor twice")

@@ -27,9 +27,12 @@ constexpr int64_t kBlock = 256;   // elements per 8-bit state block
 const at::Tensor* tensor(PyObject* o) { return o && THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
 // (a subclass that dispatches to Python, such as a tracer's, has no memory of its own)
+bool plain(const at::Tensor* t) {
+  return t && t->defined() && !t->key_set().has(c10::DispatchKey::Python) && t->layout() == at::kStrided;
+}
+
 bool fits(const at::Tensor* t, at::ScalarType type, int64_t numel, int64_t device) {
-  return t && t->defined() && !t->key_set().has(c10::DispatchKey::Python) && t->layout() == at::kStrided &&
-         t->scalar_type() == type && t->is_cuda() && t->get_device() == device && t->numel() == numel &&
+  return plain(t) && t->scalar_type() == type && t->is_cuda() && t->get_device() == device && t->numel() == numel &&
          t->is_contiguous();
 }
 
@@ -112,6 +115,11 @@ PyObject* adamw8(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(table.data()), n * 8 * (Py_ssize_t)sizeof(uint64_t));
 }
 
+// has_memory(tensor) -> whether it is a tensor with an address to ask for.
+PyObject* has_memory(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return PyBool_FromLong(na == 1 && plain(tensor(a[0])));
+}
+
 // layer(w, adapters, X, ids) -> (qlora_nf4_weight and qlora_adapter_set as bytes, M, N, K, r, count, the device's
 // current stream, whether the device is the current one), or None.  w, adapters: NF4Weight and AdapterSet.
 PyObject* layer(PyObject*, PyObject* const* a, Py_ssize_t na) {
@@ -180,6 +188,8 @@ PyMethodDef methods[] = {{"layer", reinterpret_cast<PyCFunction>(reinterpret_cas
                           "describe a layer of many adapters"},
                          {"adamw8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<adamw8>)), METH_FASTCALL,
                           "pack the tensors of an 8-bit AdamW step"},
+                         {"has_memory", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<has_memory>)),
+                          METH_FASTCALL, "whether a tensor has an address"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
