@@ -637,7 +637,7 @@ class AdamW8State:
 def _explain_adamw8(params, grads, states, masters, dev):
     """Raise the ValueError of lists that _marshal.adamw8 did not take."""
     import torch
-    seen = set()
+    written = []   # first byte, order, end, name
     for i, (p, g, s, w) in enumerate(zip(params, grads, states, masters)):
         blocks = (-(-p.numel() // ADAMW8_BLOCK),)
         _need_on(p, torch.bfloat16, p.shape, f"params[{i}]", dev)
@@ -648,12 +648,17 @@ def _explain_adamw8(params, grads, states, masters, dev):
         _need_on(s.exp_root_scale, torch.float32, blocks, f"states[{i}].exp_root_scale", dev)
         if w is not None:
             _need_on(w, torch.float32, p.shape, f"masters[{i}]", dev)
-        for t, name in ((p, "params"), (s.exp_avg, "states"), (s.exp_root, "states"), (w, "masters")):
+        for t, name in ((p, "params"), (s.exp_avg, "states"), (s.exp_root, "states"), (s.exp_avg_scale, "states"),
+                        (s.exp_root_scale, "states"), (w, "masters")):
             if t is None or not t.numel() or not _native().has_memory(t):   # (a tracer's have no address to ask for)
                 continue
-            if t.data_ptr() in seen:
-                raise ValueError(f"{name}[{i}]: the same tensor twice")
-            seen.add(t.data_ptr())
+            written.append((t.data_ptr(), len(written), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]"))
+    written.sort()
+    for (a, _, end, other), (b, _, _, name) in zip(written, written[1:]):
+        if a == b:
+            raise ValueError(f"{name}: the same tensor twice")
+        if b < end:
+            raise ValueError(f"{name}: shares memory with {other}")
     raise ValueError("params, grads, states and masters have to be lists of plain tensors")
 
 

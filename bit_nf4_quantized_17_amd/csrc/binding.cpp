@@ -6,8 +6,8 @@
 // GPU (32 parameters: about 70 us against 24 us), here a few us.  One decoded
 // token through a layer of many adapters is 10 us of GPU time; its nine
 // tensors, descriptors and stream take 6 us in Python, under one here.
-// Only well-formed arguments are packed: for anything else (a tensor or a state
-// listed twice too) the caller gets None and finds the fault and its message.
+// Only well-formed arguments are packed: for anything else (memory that two of
+// the tensors written share too) the caller gets None and finds the fault and its message.
 #define PY_SSIZE_T_CLEAN
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <exception>
+#include <utility>
 #include <vector>
 
 namespace {
@@ -80,9 +81,10 @@ PyObject* adamw8(PyObject*, PyObject* const* a, Py_ssize_t na) {
   static PyObject* const names[4] = {PyUnicode_InternFromString("exp_avg"), PyUnicode_InternFromString("exp_root"),
                                      PyUnicode_InternFromString("exp_avg_scale"),
                                      PyUnicode_InternFromString("exp_root_scale")};
-  std::vector<uint64_t> table((size_t)n * 8), seen;   // (freed if a tensor throws)
+  std::vector<uint64_t> table((size_t)n * 8);   // (freed if a tensor throws)
+  std::vector<std::pair<uint64_t, uint64_t>> written;   // first byte and end of what the step writes
   uint64_t* w = table.data();
-  seen.reserve((size_t)n * 4);
+  written.reserve((size_t)n * 6);
   bool ok = true;
   for (Py_ssize_t i = 0; ok && i < n; ++i, w += 8) {
     const at::Tensor* p = tensor(PyList_GET_ITEM(a[0], i));
@@ -107,11 +109,13 @@ PyObject* adamw8(PyObject*, PyObject* const* a, Py_ssize_t na) {
     w[1] = reinterpret_cast<uint64_t>(g->data_ptr());
     w[7] = static_cast<uint64_t>(numel);
     if (numel == 0) continue;
-    for (int k : {0, 2, 3, 6})
-      if (w[k]) seen.push_back(w[k]);
+    const uint64_t bytes[7] = {2 * w[7], 0, w[7], w[7], 4 * (uint64_t)blocks, 4 * (uint64_t)blocks, 4 * w[7]};
+    for (int k : {0, 2, 3, 4, 5, 6})
+      if (w[k]) written.emplace_back(w[k], w[k] + bytes[k]);
   }
-  std::sort(seen.begin(), seen.end());
-  if (!ok || std::adjacent_find(seen.begin(), seen.end()) != seen.end()) Py_RETURN_NONE;
+  std::sort(written.begin(), written.end());
+  const auto shared = [](const auto& x, const auto& y) { return y.first < x.second; };
+  if (!ok || std::adjacent_find(written.begin(), written.end(), shared) != written.end()) Py_RETURN_NONE;
   return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(table.data()), n * 8 * (Py_ssize_t)sizeof(uint64_t));
 }
 

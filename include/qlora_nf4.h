@@ -305,9 +305,9 @@ typedef struct {
  * up after gradients that shrink (several times too large).  A captured call
  * replays its seed and its step's bias correction: the graph is that one step.
  * Hyperparameters are doubles, each coefficient rounded to fp32 once.
- * A tensor stands in the list once, and no two share codes or scales; scales
- * need 4-byte alignment, all else 16.  step >= 1; 0 <= beta < 1; eps > 0 (a
- * variance below fp32's range is kept as zero).  count and numel may be 0
+ * No two of the buffers written (params, codes, scales, masters) share memory;
+ * scales need 4-byte alignment, all else 16.  step >= 1; 0 <= beta < 1; eps > 0
+ * (a variance below fp32's range is kept as zero).  count and numel may be 0
  * (numel at most 2^34).  A gradient of NaN or infinity makes its own element NaN:
  * the parameter, the master and, for good, both codes (0x7F).  Scales are those
  * of the finite elements, so no other element of the block changes. */
