@@ -589,9 +589,11 @@ struct NextLoads {
 };
 
 // many adapters: offsets of a row or a column that reads zeros.  A buffer ends
-// before 2^31 - 256 rows of at least 128 bytes (fits_32bit), so any valid row
-// plus COL_PAST is past it, and their sum does not wrap.
-constexpr uint32_t ROW_PAST = 0x80000000u, COL_PAST = 0x7FFF8000u;
+// 256 rows and 1024 bytes before 2^31 (fits_32bit), and a row has 16 bytes or more
+// (a dY of few columns; 8 elements), so any row plus COL_PAST is past the end, and their
+// sum does not wrap.
+constexpr uint32_t ROW_PAST = 0x80000000u, COL_PAST = 0x7FFFF000u;
+static_assert(0x80000000ull - 256 * 16 - 8 * BK * 2 <= COL_PAST && (uint64_t)ROW_PAST + COL_PAST + 8 * 16 <= 0x100000000ull);
 
 template <int MODE, bool MULTI, int TMB>
 __device__ __forceinline__ void step_pipelined(f32x16_t (&acc)[TMB][2], const u16* sA,
