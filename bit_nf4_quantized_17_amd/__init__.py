@@ -9,7 +9,8 @@ Functions keep the C ABI's names:
   nf4_levels, nf4_storage_bytes, nf4_quantize, nf4_dequantize,
   qlora_fwd_workspace_bytes, qlora_linear_fwd,
   qlora_bwd_workspace_bytes, qlora_linear_bwd, qlora_linear_bwd_noalloc,
-  qlora_multi_fwd, qlora_multi_bwd, qlora_adamw8_step, qlora_abi_version
+  qlora_multi_fwd, qlora_multi_bwd, qlora_multi_plan, qlora_adamw8_step,
+  qlora_abi_version
 """
 from __future__ import annotations
 
@@ -101,6 +102,8 @@ def lib() -> ctypes.CDLL:
     L.qlora_multi_fwd.restype = I
     L.qlora_multi_bwd.argtypes = [P, P, P, I64, P, P, I, P, P, P, P, P, SZ, P]
     L.qlora_multi_bwd.restype = I
+    L.qlora_multi_plan.argtypes = [WP, I64, I, I, ctypes.POINTER(ctypes.c_int * 3)]
+    L.qlora_multi_plan.restype = I
     L.qlora_bwd_workspace_bytes.argtypes = [I64, I64, I64, I]
     L.qlora_bwd_workspace_bytes.restype = SZ
     L.qlora_linear_bwd.argtypes = [WP, P, P, I64, P, P, I, F, I, P, P, P, P, P, SZ, P]
@@ -525,6 +528,15 @@ def qlora_multi_fwd_workspace_bytes(M: int, N: int, K: int, r: int, count: int) 
 
 def qlora_multi_bwd_workspace_bytes(M: int, N: int, K: int, r: int, count: int) -> int:
     return lib().qlora_multi_bwd_workspace_bytes(M, N, K, r, count)
+
+
+def qlora_multi_plan(w: NF4Weight, M: int, r: int, backward: bool = False) -> Tuple[str, int, int]:
+    """The kernel that the product with the weight takes for M tokens (dX's with
+    `backward`): ("stream", "fused" or "generic", rows of a tile, parts of the
+    contraction)."""
+    out = (ctypes.c_int * 3)()
+    _check(lib().qlora_multi_plan(ctypes.byref(w.descriptor()), M, r, int(backward), ctypes.byref(out)))
+    return ("stream", "fused", "generic")[out[0]], out[1], out[2]
 
 
 def _layer(w, adapters, X, ids, stream):

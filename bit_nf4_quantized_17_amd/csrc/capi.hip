@@ -560,6 +560,21 @@ int qlora_multi_fwd(const qlora_nf4_weight* w, const uint16_t* X, int64_t M, con
   return hip_status(e, "qlora_multi_fwd launch");
 }
 
+int qlora_multi_plan(const qlora_nf4_weight* w, int64_t M, int r, int backward, qlora_multi_kernel* plan) {
+  int rc = check_layer(w, M, r, QL_DTYPE_BF16);
+  if (rc) return rc;
+  if (!plan) return fail(QL_ERR_NULL, "plan is NULL");
+  const NF4View v = view(w);
+  *plan = qlora_multi_kernel{QL_MULTI_GENERIC, 128, 1};
+  if (!backward && M <= kMultiFew && multi_fwd_fits(nullptr, M, v) && multi_decode_fits(M, v, r)) {
+    *plan = qlora_multi_kernel{QL_MULTI_STREAM, 16, 1};
+  } else if (backward ? multi_dx_fits(nullptr, (v.N + 7) / 8 * 8, M, v) : multi_fwd_fits(nullptr, M, v)) {
+    plan->kernel = QL_MULTI_FUSED;
+    multi_tiles(M, backward ? v.K : v.N, backward ? v.N : v.K, &plan->rows, &plan->parts);
+  }
+  return ok();
+}
+
 size_t qlora_multi_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int count) {
   return multi_sizes_ok(M, N, K, r, count) ? multi_layout(M, N, K, r, count, true).total : 0;
 }

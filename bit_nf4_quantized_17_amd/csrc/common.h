@@ -236,6 +236,10 @@ hipError_t launch_multi_fwd(const MultiOrder& mo, const NF4View& w, const u16* X
 hipError_t launch_multi_dx(const MultiOrder& mo, const NF4View& w, const u16* dY, int64_t ldy, int64_t M,
                            const float* U, const u16* A, int r, float* ws, u16* dX, hipStream_t st);
 int64_t multi_main_elems(int64_t M, int64_t J, int64_t C);
+// whether launch_multi_dx takes a shape itself
+bool multi_dx_fits(const u16* dY, int64_t ldy, int64_t M, const NF4View& w);
+// rows of a tile and parts of the contraction that the fused kernel takes
+void multi_tiles(int64_t M, int64_t J, int64_t C, int* rows, int* parts);
 hipError_t launch_multi_fwd_generic(const MultiOrder& mo, const NF4View& w, const u16* X, int64_t M, const float* T,
                                     const u16* B, int r, u16* Y, hipStream_t st);
 hipError_t launch_multi_dx_generic(const MultiOrder& mo, const NF4View& w, const u16* dY, int64_t ldy, int64_t M,

@@ -1168,6 +1168,16 @@ int64_t multi_main_elems(int64_t M, int64_t J, int64_t C) {
   return pl.splits > 1 ? pl.splits * M * J : 0;
 }
 
+void multi_tiles(int64_t M, int64_t J, int64_t C, int* rows, int* parts) {
+  const big::MultiPlan pl = big::multi_plan(M, J, C);
+  *rows = 64 * pl.tmb;
+  *parts = pl.splits;
+}
+
+bool multi_dx_fits(const u16* dY, int64_t ldy, int64_t M, const NF4View& w) {
+  return big::vec_ok(dY, ldy) && fits_32bit(M, ldy, w) && (w.N + big::BK) * w.K / 2 < ((int64_t)1 << 31);
+}
+
 // whether launch_multi_fwd takes a shape itself
 bool multi_fwd_fits(const u16* X, int64_t M, const NF4View& w) { return big::vec_ok(X, w.K) && fits_32bit(M, w.K, w); }
 
@@ -1190,7 +1200,7 @@ hipError_t launch_multi_fwd(const MultiOrder& mo, const NF4View& w, const u16* X
 
 hipError_t launch_multi_dx(const MultiOrder& mo, const NF4View& w, const u16* dY, int64_t ldy, int64_t M,
                            const float* U, const u16* A, int r, float* ws, u16* dX, hipStream_t st) {
-  if (!big::vec_ok(dY, ldy) || !fits_32bit(M, ldy, w) || (w.N + big::BK) * w.K / 2 >= ((int64_t)1 << 31))
+  if (!multi_dx_fits(dY, ldy, M, w))
     return launch_multi_dx_generic(mo, w, dY, ldy, M, U, A, r, dX, st);
   big::BigArgs p{};
   p.a = dY; p.lda = ldy; p.a_vec = true;

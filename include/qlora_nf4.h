@@ -365,6 +365,21 @@ int qlora_multi_bwd(const qlora_nf4_weight* w, const uint16_t* X, const uint16_t
                     const float* T_saved, uint16_t* dX, uint16_t* dA, uint16_t* dB,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* Which kernel a many-adapter call's product with the weight takes (forward, or
+ * with backward != 0 dX): the weight stream (up to 16 tokens, 8-bit scales), the
+ * fused tiles of 64, 128 or 256 rows with the contraction in `parts`, or the
+ * generic tiles (operands of 2 GiB and more).  Host only; w's buffers are not
+ * read. */
+#define QL_MULTI_STREAM 0
+#define QL_MULTI_FUSED 1
+#define QL_MULTI_GENERIC 2
+typedef struct {
+  int kernel;
+  int rows;
+  int parts;
+} qlora_multi_kernel;
+int qlora_multi_plan(const qlora_nf4_weight* w, int64_t M, int r, int backward, qlora_multi_kernel* plan);
+
 /* Workspace the backward needs (bytes, 256-byte granular). */
 size_t qlora_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
 
