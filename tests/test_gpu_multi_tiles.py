@@ -48,6 +48,7 @@ FWD = [
     (700, 11008, 64, 100, 3, "mixed", 256, False),
     (1030, 8000, 64, 8, 300, "distinct", 256, False),
     (1030, 8001, 64, 9, 300, "distinct", 256, False),
+    (1030, 8000, 64, 8, 1030, "distinct", 256, False),   # every row its own run
     (129, 11008, 2048, 128, 3, "mixed", 256, True),
     (129, 11007, 2048, 12, 60, "distinct", 256, True),
     (513, 8000, 64, 64, 5, "mixed", 128, False),
