@@ -61,8 +61,9 @@
 // before.  K is any multiple of 64 here: a row may end in half a chunk, whose
 // second block meets zero activations and zero scales (4 tokens, 5019x2688:
 // 17 us, 37 through the tiled kernel).  Bound by the weight's stream as with one
-// adapter: 16 requests on 8192^2, r = 16, 4.6 us for T and 20.9 us; one token on
-// 4096^2 3.8 and 8.0 us, two launches' latency.
+// adapter: 16 requests on 8192^2, r = 16, 3.8 us for T and 21.2 us; one token on
+// 4096^2 3.8 and 8.2 us, of which an empty launch is 1.5: T ends before the
+// stream starts, and the stream takes T and the factors in before its first tile.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

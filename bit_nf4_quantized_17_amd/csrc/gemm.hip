@@ -1077,9 +1077,11 @@ static SkinnyPlan multi_rows_plan(int64_t M, int64_t C, int count, int64_t most)
   const int64_t per = cdiv(ctiles, splits) * BK;
   return SkinnyPlan{(int)cdiv(C, per), per};
 }
-// T: up to eight slices that every column tile reads again, 16 MB in all, cost
-// less than a launch that adds them up first (about 5 us; 45 slices of 318
-// tokens cost 60 us).  A short contraction (40 stages) is cut into eight for it.
+// T: up to eight slices that every column tile reads again, 16 MB in all, are
+// added up by the fused kernel, for a launch less (333 tokens, 1000x1984, r = 12: a
+// call 32.7 us for 33.8); with more of them the launch is cheaper (520 tokens,
+// 4096^2, r = 64: 60 us for 72 in the kernel; 318, 11008x8192: 139 for 203).  A
+// short contraction (40 stages) is cut into eight for it: 32.7 us for 34.1.
 static bool t_sliced(int64_t slices, int64_t M, int64_t N, int r) {
   return slices <= 8 && slices * M * r * 4 * cdiv(N, 256) <= (int64_t)16 << 20;
 }
@@ -1091,8 +1093,9 @@ bool multi_t_sliced(int64_t M, int64_t N, int64_t K, int r, int count) {
 }
 // dA and dB: the longest piece of an adapter's tokens, so that the pieces of
 // evenly cut tokens fill the chip about twice (kSkinnyWorkgroups), at least 256
-// (with 128: 1030 tokens, 4096^2, r = 64 20.0 us for 18.0 with the pieces' sums
-// added up, 2000 tokens, 2048^2, r = 100 42.4 for 39.0, 300 tokens 10.0 for 8.0)
+// (a backward with 128, 256, 512: 1030 tokens, 4096^2, r = 64 99.9, 97.3, 100.6 us;
+// 2000 tokens, 2048^2, r = 100 92.0, 89.7, 99.7; 777, 1003x832, r = 3 48.5, 48.2,
+// 44.9)
 static int64_t segs_step(int64_t I, int64_t M) {
   const int64_t nt = std::max<int64_t>(1, std::min<int64_t>({cdiv(kSkinnyWorkgroups, cdiv(I, 128)), M / 256, 64}));
   return cdiv(cdiv(M, nt), BK) * BK;

@@ -53,8 +53,9 @@
 // factor holds.  For the same reason main-loop loads past the contraction's end
 // read zeros here (elsewhere they read into the next row and meet zero
 // weights, which is the same for finite values).  4096 tokens of 16 adapters, r =
-// 64, 28672x8192: 1.70 ms, 1.13 PFLOP/s, within 3% of one adapter's kernel and
-// bound as it is; 8192 tokens, dX of 11008x4096: 0.65 ms, 1.14 PFLOP/s.
+// 64, 28672x8192: 1.70-1.84 ms from card to card, 1.05-1.13 PFLOP/s, bound as one
+// adapter's kernel is; 8192 tokens, dX of 11008x4096: 0.65-0.70 ms, 1.05-1.14
+// PFLOP/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1034,12 +1035,17 @@ __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, in
 // Tile rows (64 TMB) and parts of the contraction for M x J outputs over C:
 // the least of rounds of workgroups x steps x step time, plus joining the
 // parts' sums (8 bytes an output and part at 4 TB/s).  A step of 64 (MI355X,
-// r = 16, 16 shapes of 32 to 4096 tokens on 4096^2 to 28672x8192 weights
-// measured with every tile and split) takes 0.85, 1.0, 1.3 us for 64, 128 and
-// 256 rows with few workgroups, 1.1, 1.4, 1.95 us with one on every compute
-// unit; choosing by these was within 1% of the best measured on each.  Few
-// rows take small tiles (64 x 28672x8192: 95 us against 126 us with 256-row
-// tiles), few tiles split (64 x 8192^2: 50 us in 8 parts, 128 us whole).
+// 256 compute units, r = 16, shapes of 32 to 4096 tokens on 4096^2 to 28672x8192
+// weights) takes 0.85, 1.0, 1.3 us for 64, 128 and 256 rows with few workgroups,
+// 1.1, 1.4, 1.95 us with one on every compute unit.  A choice, not a
+// prediction: the constant 4 us stands for a prologue that grows with the runs
+// of a tile, the rank and T's slices, so a kernel of few steps takes up to 2.5
+// times the sum (56 tokens of 30 adapters, r = 64: 32 us for 19; 4001 tokens,
+// 344-369 for 339).  That cancels where tiles and parts are compared: of 20 calls
+// timed at every tile and split (r = 3 to 128, up to 100 adapters) 15 had the
+// best, 5 were 3-8% over it, three of them at 200 tokens.  Few rows take small
+// tiles (64 x 28672x8192: 95 us against 126 us with 256-row tiles), few tiles
+// split (64 x 8192^2: 50 us in 8 parts, 128 us whole).
 struct MultiPlan {
   int tmb, splits, kt_per;
 };

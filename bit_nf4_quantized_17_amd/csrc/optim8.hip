@@ -31,8 +31,9 @@
 // block, bound by HBM.  32 lanes hold a block, 8 elements a lane, so a block's
 // largest values are one reduction over half a wave; one workgroup handles 8
 // blocks of one tensor, and a launch covers up to MAXT tensors.  70.8M parameters
-// in 60 tensors: 147 us in two launches, 4.8 TB/s (a large copy: 5.15); 8.0M
-// with masters in 32 tensors: 23.6 us; 0.5M in 8: 4.9 us, a launch's latency.
+// in 60 tensors: 146 us in two launches, 4.9 TB/s (a large copy: 5.2); 8.0M
+// with masters in 32 tensors: 24.9 us; 0.5M in 8: 5.4 us, one chain of loads,
+// reduction and stores in one round of workgroups (an empty launch: 1.5).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
